@@ -106,11 +106,15 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
     tmax = team_max<NT>(e.t, l);
     if (tmax == -__builtin_inff()) tmax = 0.f;
   }
+  const bool listed = TAIL && team_any<NT>(e.id != -1, l);
   const double tscale = TAIL ? 1.0 : a.inv_t;
   const double u = ((double)e.t - (double)tmax) * tscale;
   double q = e.id != -1 ? exp(u) : 0.0;
   team_sync<NT>();
   const double qsum = team_sum<NT>(q, l);
+  // Nothing listed, or (without the tail) every entry of zero probability: no
+  // teacher, and neither loss nor gradient whatever the logits hold.
+  const bool teacher = TAIL ? listed : qsum != 0.0;
   const double t2 = exponent64(x, e.z);
   double sum = r.s;
   if (TAIL) {
@@ -119,7 +123,7 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
     sum += team_sum<NT>(first && e.id >= 0 ? (double)hw_exp2((float)t2) : 0.0, l);
   }
   const bool none = sum == 0.0 && r.m == -__builtin_inff();
-  double rest = TAIL ? 1.0 - qsum : 0.0;
+  double rest = TAIL && teacher ? 1.0 - qsum : 0.0;
   if (rest < 0.0) rest = 0.0;
   const double left = TAIL && !none ? r.s / sum : 0.0;
   // One evaluation of the logarithm, on four lanes.
@@ -129,9 +133,8 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   const double logp = none ? -kInf : kLn2 * t2 - ln_s;
   double logq = u, qscale = 1.0;
   if (!TAIL) {
-    // Nothing listed, or every entry of zero probability: no teacher, no loss.
-    qscale = qsum == 0.0 ? 0.0 : 1.0 / qsum;
-    logq = u - (qsum == 0.0 ? 0.0 : lane_value(lns, 1));
+    qscale = teacher ? 1.0 / qsum : 0.0;
+    logq = u - (teacher ? lane_value(lns, 1) : 0.0);
     q *= qscale;
   }
   q32 = (float)q;
@@ -139,8 +142,8 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   if (e.id == -2) part = __builtin_nan("");
   team_sync<NT>();
   double loss = team_sum<NT>(part, l);
-  double off = qscale == 0.0 ? 0.0 : 1.0;
-  if (TAIL) {
+  double off = teacher ? 1.0 : 0.0;
+  if (TAIL && teacher) {
     if (left == 0.0 && !none) {
       // Nothing off the list for the rest to fall on: what the rounding of
       // the list's values (half a step of their type each) can make of a
@@ -158,7 +161,7 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   if (none) qscale = 0.0;
   // (off / sum is at most the reciprocal of the smallest exponential, 2^126.)
   const float inv_s = none ? 0.f : (float)(1.0 / sum);
-  const DistillStats st{x.ref, inv_s, none ? 0.f : (float)(off / sum), tmax, (float)tscale,
+  const DistillStats st{x.ref, inv_s, none || off == 0.0 ? 0.f : (float)(off / sum), tmax, (float)tscale,
                         (float)qscale, x.far ? 1.f : 0.f, 0.f};
   if (tid == 0) {
     a.loss[row] = (float)loss;
@@ -180,7 +183,7 @@ __device__ __forceinline__ void distill_grad(const DistillArgs& a, uint32_t row,
   const E* z = part.z;
   E* out = static_cast<E*>(a.grad) + (size_t)row * a.in.V + part.lo;
   const float w = (a.weight ? a.weight[(size_t)row * a.w_step] : 1.f) * (float)a.inv_t;
-  const float on = w * st.inv_s, A = w * st.off;
+  const float on = w * st.inv_s, A = st.off == 0.f ? 0.f : w * st.off;
   const Exponent ex{a.c, st.ref, st.far != 0.f};
   auto write = [&](auto value) {
     auto group = [&](const Group<E>& g, uint32_t base) {

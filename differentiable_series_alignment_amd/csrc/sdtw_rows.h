@@ -457,6 +457,16 @@ template <int NT> __device__ __forceinline__ float team_max(float v, ReduceLds<N
   for (int i = 1; i < NT / kWave; ++i) v = fmaxf(v, l.m[i]);
   return v;
 }
+template <int NT> __device__ __forceinline__ bool team_any(bool v, ReduceLds<NT>& l) {
+  v = __builtin_amdgcn_ballot_w64(v) != 0;
+  if (NT == kWave) return v;
+  if (lane_id() == 0) l.w[threadIdx.x / kWave] = v ? 1.0 : 0.0;
+  __syncthreads();
+  v = l.w[0] != 0.0;
+#pragma unroll
+  for (int i = 1; i < NT / kWave; ++i) v |= l.w[i] != 0.0;
+  return v;
+}
 template <int NT> __device__ __forceinline__ double team_sum(double v, ReduceLds<NT>& l) {
   v = wave_sum(v);
   if (NT == kWave) return v;

@@ -361,8 +361,9 @@ def distillation_loss(logits: torch.Tensor, teacher_tokens: torch.Tensor,
     list.  The factor temperature^2 that some recipes apply is the caller's.
 
     Differentiable in the logits; the teacher is constant.  An id listed twice
-    adds in q and counts once in p; a row without entries has loss 0; an id
-    outside the vocabulary makes its row NaN."""
+    adds in q and counts once in p; an id outside the vocabulary makes its row
+    NaN.  A row without entries has loss 0 and gradient 0, whatever its logits
+    hold."""
     t = _check_distill(logits, teacher_tokens, teacher_logits, temperature)
     if torch.is_grad_enabled() and logits.requires_grad:
         return _DistillationFunction.apply(logits, teacher_tokens, teacher_logits, t,

@@ -259,7 +259,9 @@ int sdtw_timing_collect(const char **names, float *ms, int cap);
  *    is what a forward leaves for the gradient.
  *  - Logits of -inf are entries of probability zero.  A row with nothing
  *    above -inf has no distribution: log-probabilities -inf, entropy 0,
- *    gradient 0.  A NaN or +inf in a row makes that row's results NaN.
+ *    gradient 0.  A NaN or +inf in a row makes that row's results NaN, but
+ *    for what does not depend on the logits (the log-probability of an ignored
+ *    token, a distillation row without entries).
  *  - A token or id equal to ignore_index is padding; any other one outside
  *    [0, V) makes the results of its row NaN (nothing is read or written
  *    there).
@@ -324,7 +326,9 @@ size_t sdtw_distill_workspace_bytes(int64_t B, int64_t N, int64_t V, int K);
  *     p_r the probability off the list (below fp32's range it is zero; where
  *     it is zero, a q_r that the rounding of the values explains is too).
  * An id listed twice adds in q and counts once in p.  A row without entries
- * has loss 0 and gradient 0.
+ * (nothing but padding; with tail = 0 also values of -inf alone) has loss 0
+ * and gradient 0 whatever its logits, -inf, +inf and NaN among them, and
+ * whatever its upstream gradient.
  * loss != NULL: writes loss [B,N] (fp32) and, if given, stats ([B,N,8] fp32).
  * grad_logits != NULL: writes the gradient ([B,N,V] contiguous, of `dtype`)
  *   for upstream gradients grad_loss (fp32, one value a row, gl_step apart:
