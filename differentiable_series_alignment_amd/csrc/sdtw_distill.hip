@@ -13,7 +13,11 @@
 // An id that stands twice in a list counts once in p and adds in q.  p_r is
 // summed over the entries off the list themselves (a difference from one
 // would lose it where the student is sure of the list): a bitmap of the list
-// in LDS costs one byte's read for each vector of logits.  The loss is a
+// in LDS costs one byte's read for each vector of logits.  Their exponents'
+// reference is their own maximum, m_r, so that neither p_r nor its logarithm is
+// ever too small for the numbers they are held in: with S_r their sum,
+//   p_r = S_r 2^(m_r - m) / S,  T dL/dz_j = 2^(t_j - m_r) (p_r - q_r) / S_r.
+// The loss is a
 // small difference of logarithms once the student is near the teacher, so
 // the sums and the list's few values are fp64.
 #include "sdtw.h"
@@ -30,11 +34,11 @@ constexpr int kListWave = 64;   // of a team of one wave
 struct alignas(16) DistillStats {
   float ref;      // reference of the exponents
   float inv_s;    // 1 / sum of the row (0: no entry above -inf)
-  float off;      // inv_s times the factor of p off the list (NaN: a bad id)
+  float off;      // factor of 2^t off the list (NaN: a bad id)
   float tmax;     // q = e^((t - tmax) * tscale) * qscale
   float tscale, qscale;
-  float far;      // 1: exponents as (z - ref) c
-  float unused;
+  float far;      // exponents as (z - ref) c: 1 against ref, 2 against off_ref
+  float off_ref;  // reference of the exponents off the list
 };
 
 struct DistillArgs {
@@ -92,21 +96,26 @@ __device__ __forceinline__ ListEntry list_entry(const DistillArgs& a, uint32_t r
 
 // Loss and statistics of a row by a team, thread k with the list's k-th entry
 // (`first`: the first, or only, entry of its id), from the row's maximum and
-// its sum (without the list's entries if TAIL).  Returns the statistics and
-// the thread's q.
+// its sum (those of the entries off the list if TAIL).  Returns the statistics
+// and the thread's q.
 template <typename E, bool TAIL, int NT>
 __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uint32_t row,
                                                        RowSums r, const ListEntry& e, bool first,
                                                        float& q32, ReduceLds<NT>& l) {
   const int tid = team_tid<NT>();
-  const Exponent x = row_exponent(r.m, a.c);
-  // fmax passes over a NaN of the teacher; the sum below meets it again.
-  float tmax = 0.f;
-  if (!TAIL) {
+  // fmax passes over a NaN of the teacher, or of the listed logits; the sums
+  // below meet it again.
+  float tmax = 0.f, m = r.m;
+  bool listed = false;
+  if (TAIL) {
+    const ListTop t = team_list<NT>(e.id >= 0 ? e.z : -__builtin_inff(), e.id != -1, l);
+    m = fmaxf(m, t.m);
+    listed = t.any;
+  } else {
     tmax = team_max<NT>(e.t, l);
     if (tmax == -__builtin_inff()) tmax = 0.f;
   }
-  const bool listed = TAIL && team_any<NT>(e.id != -1, l);
+  const Exponent x = row_exponent(m, a.c), y = TAIL ? row_exponent(r.m, a.c) : x;
   const double tscale = TAIL ? 1.0 : a.inv_t;
   const double u = ((double)e.t - (double)tmax) * tscale;
   double q = e.id != -1 ? exp(u) : 0.0;
@@ -116,19 +125,22 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   // teacher, and neither loss nor gradient whatever the logits hold.
   const bool teacher = TAIL ? listed : qsum != 0.0;
   const double t2 = exponent64(x, e.z);
-  double sum = r.s;
+  double sum = r.s, share = r.s, down = 0.0;
   if (TAIL) {
-    // The list's own share of the row, every id once.
+    // The share of the entries off the list (none of them above -inf: zero, or
+    // NaN), and the list's own, every id once.
+    down = reference64(r.m, a.c) - reference64(m, a.c);
+    if (r.m != -__builtin_inff()) share *= exp2_wide(down);
     team_sync<NT>();
-    sum += team_sum<NT>(first && e.id >= 0 ? (double)hw_exp2((float)t2) : 0.0, l);
+    sum = share + team_sum<NT>(first && e.id >= 0 ? (double)hw_exp2((float)t2) : 0.0, l);
   }
-  const bool none = sum == 0.0 && r.m == -__builtin_inff();
+  const bool none = sum == 0.0 && m == -__builtin_inff();
   double rest = TAIL && teacher ? 1.0 - qsum : 0.0;
   if (rest < 0.0) rest = 0.0;
-  const double left = TAIL && !none ? r.s / sum : 0.0;
+  const double left = TAIL && !none ? share / sum : 0.0;
   // One evaluation of the logarithm, on four lanes.
   const int lane = lane_id();
-  const double lns = log(lane == 0 ? sum : lane == 1 ? qsum : lane == 2 ? rest : left);
+  const double lns = log(lane == 0 ? sum : lane == 1 ? qsum : lane == 2 ? rest : r.s);
   const double ln_s = none ? 0.0 : lane_value(lns, 0);
   const double logp = none ? -kInf : kLn2 * t2 - ln_s;
   double logq = u, qscale = 1.0;
@@ -142,27 +154,27 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   if (e.id == -2) part = __builtin_nan("");
   team_sync<NT>();
   double loss = team_sum<NT>(part, l);
-  double off = teacher ? 1.0 : 0.0;
+  double off = none || !teacher ? 0.0 : 1.0 / sum;
   if (TAIL && teacher) {
-    if (left == 0.0 && !none) {
-      // Nothing off the list for the rest to fall on: what the rounding of
-      // the list's values (half a step of their type each) can make of a
+    if (left < 0x1p-126 && !none) {
+      // Next to nothing off the list for the rest to fall on: what the rounding
+      // of the list's values (half a step of their type each) can make of a
       // list that is complete is no rest.
       const double half = a.list.bytes == SDTW_DTYPE_F32    ? 0x1p-24
                           : a.list.bytes == SDTW_DTYPE_BF16 ? 0x1p-8 : 0x1p-11;
       team_sync<NT>();
       if (rest <= half * (1.0 + team_sum<NT>(q == 0.0 ? 0.0 : q * fabs(logq), l))) rest = 0.0;
     }
-    if (rest != 0.0) loss += rest * (lane_value(lns, 2) - (none ? -kInf : lane_value(lns, 3)));
-    // No probability off the list: none to scale.
-    off = rest == 0.0 ? 1.0 : left == 0.0 ? 0.0 : 1.0 - rest / left;
+    if (rest != 0.0)
+      loss += rest * (lane_value(lns, 2) - (lane_value(lns, 3) + kLn2 * down - ln_s));
+    // (No entry off the list: nothing to scale.)
+    off = r.s == 0.0 ? 0.0 : (left - rest) / r.s;
   }
   if (__builtin_isnan(loss)) off = __builtin_nan("");
   if (none) qscale = 0.0;
-  // (off / sum is at most the reciprocal of the smallest exponential, 2^126.)
   const float inv_s = none ? 0.f : (float)(1.0 / sum);
-  const DistillStats st{x.ref, inv_s, none || off == 0.0 ? 0.f : (float)(off / sum), tmax, (float)tscale,
-                        (float)qscale, x.far ? 1.f : 0.f, 0.f};
+  const DistillStats st{x.ref, inv_s, none ? 0.f : (float)off, tmax, (float)tscale,
+                        (float)qscale, (x.far ? 1.f : 0.f) + (y.far ? 2.f : 0.f), y.ref};
   if (tid == 0) {
     a.loss[row] = (float)loss;
     if (a.stats) a.stats[row] = st;
@@ -170,8 +182,9 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   return st;
 }
 
-// Writes the gradient of a part of a row, first as of entries off the list,
-// then the list's own.  `id` is the calling thread's entry of the
+// Writes the gradient of a part of a row, first as of entries off the list
+// (whose reference a listed entry may exceed by any amount: what is written for
+// it is whatever comes of that), then the list's own.  `id` is the calling thread's entry of the
 // list (-1: none), whose ids and probabilities are in l behind a team_sync.
 // The first HG groups (ALL: there are no more) are in `held` already.
 template <typename E, int NT, bool ONCE, int HG, bool ALL>
@@ -184,7 +197,8 @@ __device__ __forceinline__ void distill_grad(const DistillArgs& a, uint32_t row,
   E* out = static_cast<E*>(a.grad) + (size_t)row * a.in.V + part.lo;
   const float w = (a.weight ? a.weight[(size_t)row * a.w_step] : 1.f) * (float)a.inv_t;
   const float on = w * st.inv_s, A = st.off == 0.f ? 0.f : w * st.off;
-  const Exponent ex{a.c, st.ref, st.far != 0.f};
+  const Exponent on_list{a.c, st.ref, st.far == 1.f || st.far == 3.f};
+  const Exponent ex{a.c, st.off_ref, st.far >= 2.f};
   auto write = [&](auto value) {
     auto group = [&](const Group<E>& g, uint32_t base) {
 #pragma unroll
@@ -209,12 +223,7 @@ __device__ __forceinline__ void distill_grad(const DistillArgs& a, uint32_t row,
     if (rest < part.len) out[rest] = (E)value((float)z[rest]);
   };
   // A row of no weight, or whose entries off the list have no gradient.
-  // Weights of a scaled loss can carry the factor of a student that is sure of
-  // the list past fp32; its product with an exponential is at most their sum.
   if (w == 0.f || A == 0.f) write([](float) { return 0.f; });
-  else if (__builtin_isinf(A)) write([&](float x) {
-    return hw_exp2(ex.far ? exponent<true>(ex, x) : exponent<false>(ex, x)) * st.off * w;
-  });
   else if (ex.far) write([&](float x) { return hw_exp2(exponent<true>(ex, x)) * A; });
   else write([&](float x) { return hw_exp2(exponent<false>(ex, x)) * A; });
   team_sync<NT>();
@@ -224,7 +233,7 @@ __device__ __forceinline__ void distill_grad(const DistillArgs& a, uint32_t row,
     float q = 0.f;                      // every entry of the same id writes the same sum
     for (int j = 0; j < a.K; ++j) q += l.ids[j] == id ? l.q[j] : 0.f;
     const float x = (float)z[id - lo];
-    const float t = ex.far ? exponent<true>(ex, x) : exponent<false>(ex, x);
+    const float t = on_list.far ? exponent<true>(on_list, x) : exponent<false>(on_list, x);
     out[id - lo] = (E)(hw_exp2(t) * on - w * q);
   }
 }

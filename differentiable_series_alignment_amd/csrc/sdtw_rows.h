@@ -230,38 +230,17 @@ __device__ __forceinline__ void term_add(const Exponent& x, float z, float& s, f
   if (W) w = __builtin_fmaf(e, fmaxf(t, -200.f), w);   // 0 * -inf is no NaN
 }
 
-// Adds a group.  LISTED: skip(u) has a bit for each entry of vector u that
-// stays out, few of them: a wave takes a vector with selects where any of its
-// lanes has such an entry, else without (selects for all cost two to four
-// operations an entry beside its fma, exponential and sum: 53 us for 2048 rows
-// of 50016 bf16 entries, 44 so).
-template <typename E, bool W, bool LISTED, typename Skip>
-__device__ __forceinline__ void group_add(RowSums& r, const Exponent& x, const Group<E>& g,
-                                          Skip skip) {
+// Adds a group.
+template <typename E, bool W>
+__device__ __forceinline__ void group_add(RowSums& r, const Exponent& x, const Group<E>& g) {
   constexpr int U = kRowUnroll<E>, n = kRowVec<E>;
   float s = 0.f, w = 0.f;
-  unsigned out[U];
-  bool some[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) out[u] = LISTED ? skip(u) : 0u;
-#pragma unroll
-  for (int u = 0; u < U; ++u) some[u] = LISTED && __builtin_amdgcn_ballot_w64(out[u] != 0) != 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const auto z = row_wide<E>(g.v[u]);
     float su = 0.f, wu = 0.f;
-    if (LISTED && some[u]) {
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        float zi = z[i];
-        asm volatile("" : "+v"(zi));      // (or the selects go into both branches)
-        const float e = hw_exp2(exponent<false>(x, zi));
-        su += out[u] >> i & 1u ? 0.f : e;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < n; ++i) term_add<W, false>(x, z[i], su, wu);
-    }
+    for (int i = 0; i < n; ++i) term_add<W, false>(x, z[i], su, wu);
     s += su;
     if (W) w += wu;
   }
@@ -282,6 +261,40 @@ template <typename E>
 __device__ __forceinline__ bool is_listed(const uint32_t* listed, const Part<E>& p, uint32_t i) {
   const uint32_t bit = p.bit(i);
   return listed[bit >> 5] >> (bit & 31) & 1u;
+}
+// Entry i of a vector to -inf where bit i of `out` is set.
+template <typename E>
+__device__ __forceinline__ typename RowType<E>::Raw vector_leave(typename RowType<E>::Raw v,
+                                                                 unsigned out) {
+  typedef unsigned Words __attribute__((ext_vector_type(4)));
+  constexpr unsigned none = sizeof(E) == 4                    ? 0xFF800000u
+                            : std::is_same<E, __bf16>::value  ? 0xFF80FF80u
+                                                              : 0xFC00FC00u;
+  Words w = __builtin_bit_cast(Words, v);
+  auto bit = [&](int i) { return (unsigned)((int)(out << (31 - i)) >> 31); };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned m = sizeof(E) == 4 ? bit(k) : (bit(2 * k) & 0xFFFFu) | (bit(2 * k + 1) & ~0xFFFFu);
+    w[k] = (none & m) | (w[k] & ~m);
+  }
+  return __builtin_bit_cast(typename RowType<E>::Raw, w);
+}
+// A group from vector `base` on without its listed entries (-inf in their
+// place), few of them: a wave changes a vector where any of its lanes has one
+// (selects for all cost two to four operations an entry beside its fma,
+// exponential and sum).
+template <typename E, int NT>
+__device__ __forceinline__ void group_leave(Group<E>& g, uint32_t base, const uint32_t* listed,
+                                            const Part<E>& p) {
+  constexpr int U = kRowUnroll<E>;
+  unsigned out[U];
+  // (Behind the last vector there are none, whatever the bits.)
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    out[u] = listed_bits<E>(listed, p, min(base + u * NT + team_tid<NT>(), p.nvec - 1));
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (__builtin_amdgcn_ballot_w64(out[u] != 0) != 0) g.v[u] = vector_leave<E>(g.v[u], out[u]);
 }
 
 // A part's first groups, requested before anything else is done for the row:
@@ -328,9 +341,10 @@ __device__ __forceinline__ void each_group(const E* p, uint32_t base, uint32_t n
 
 // A part of a row by a team: group g holds vectors [g U NT, (g + 1) U NT) of
 // the part; the entries before and behind the vectors belong to threads 0, 1,
-// ...  With LISTED the entries in the bitmap stay out of the sums (not of the
-// maximum).  gmax, if not null, gets the maximum of each thread's groups,
-// [groups][NT].  `start`: what row_start requested; its held groups stay.
+// ...  With LISTED the entries in the bitmap stay out of the sums and of the
+// maximum.  gmax, if not null, gets the maximum of each thread's groups,
+// [groups][NT].  `start`: what row_start requested; its held groups stay
+// (listed entries as -inf).
 template <typename E, int NT, bool W, bool LISTED, bool ONCE, int HG, bool ALL>
 __device__ __forceinline__ RowSums row_sums(const Part<E>& part, float c, const uint32_t* listed,
                                             float* gmax, RowStart<E, HG>& start) {
@@ -339,8 +353,9 @@ __device__ __forceinline__ RowSums row_sums(const Part<E>& part, float c, const 
   const uint32_t nvec = part.nvec, tid = team_tid<NT>();
   const E* p = part.vectors();
   RowSums r{-__builtin_inff(), 0.0, 0.0};
-  auto add = [&](const Group<E>& whole, uint32_t base) {
-    const Group<E> g = group_cut<E, NT>(whole, base, nvec);
+  auto add = [&](Group<E>& g, uint32_t base) {
+    g = group_cut<E, NT>(g, base, nvec);
+    if (LISTED) group_leave<E, NT>(g, base, listed, part);
     const float m = group_max<E>(g);
     if (gmax) gmax[base / kRowUnroll<E> + tid] = m;
     if (m > r.m) sums_move<W>(r, c, m);
@@ -351,25 +366,20 @@ __device__ __forceinline__ RowSums row_sums(const Part<E>& part, float c, const 
     if (sizeof(E) == 2 && (HG > 1 || LISTED))
 #pragma unroll
       for (int u = 0; u < kRowUnroll<E>; ++u) asm volatile("" : "+v"(again.v[u]));
-    group_add<E, W, LISTED>(r, x, again, [&](int u) -> unsigned {
-      // (Behind the last vector every exponential is zero, whatever the bits.)
-      return listed_bits<E>(listed, part, min(base + u * NT + tid, nvec - 1));
-    });
+    group_add<E, W>(r, x, again);
   };
 #pragma unroll
   for (int h = 0; h < HG; ++h)
     if (h * step < nvec) add(start.held[h], h * step);
   if (!ALL) each_group<E, NT, ONCE>(p, HG * step, nvec, start.a, start.b, add);
   const uint32_t rest = part.rest(tid);
-  if (rest < part.len) {
+  if (rest < part.len && !(LISTED && is_listed<E>(listed, part, rest))) {
     const float v = (float)part.z[rest];
     if (v > r.m) sums_move<W>(r, c, v);
-    if (!(LISTED && is_listed<E>(listed, part, rest))) {
-      float s = 0.f, w = 0.f;
-      term_add<W, false>(Exponent{c, reference(r.m, c), false}, v, s, w);
-      r.s += (double)s;
-      if (W) r.w += (double)w;
-    }
+    float s = 0.f, w = 0.f;
+    term_add<W, false>(Exponent{c, reference(r.m, c), false}, v, s, w);
+    r.s += (double)s;
+    if (W) r.w += (double)w;
   }
   return r;
 }
@@ -395,6 +405,17 @@ __device__ __forceinline__ bool far_row(float m, float c) {
 __device__ __forceinline__ Exponent row_exponent(float m, float c) {
   const bool far = far_row(m, c);
   return Exponent{c, far ? m : reference(m, c), far};
+}
+
+// The reference of a row, or part, of maximum m in fp64, far or not.
+__device__ __forceinline__ double reference64(float m, float c) {
+  return far_row(m, c) ? (double)m * (double)c : (double)reference(m, c);
+}
+// 2^d for d <= 0 to fp32's accuracy in fp64's range.
+__device__ __forceinline__ double exp2_wide(double d) {
+  d = fmin(fmax(d, -2000.0), 0.0);
+  const double n = rint(d);
+  return ldexp((double)hw_exp2((float)(d - n)), (int)n);
 }
 
 // ln of a positive fp64 number to about 5e-8: the exponent apart, and fp32's
@@ -457,15 +478,27 @@ template <int NT> __device__ __forceinline__ float team_max(float v, ReduceLds<N
   for (int i = 1; i < NT / kWave; ++i) v = fmaxf(v, l.m[i]);
   return v;
 }
-template <int NT> __device__ __forceinline__ bool team_any(bool v, ReduceLds<NT>& l) {
-  v = __builtin_amdgcn_ballot_w64(v) != 0;
-  if (NT == kWave) return v;
-  if (lane_id() == 0) l.w[threadIdx.x / kWave] = v ? 1.0 : 0.0;
+// The maximum of v and whether `any` is true anywhere.
+struct ListTop {
+  float m;
+  bool any;
+};
+template <int NT>
+__device__ __forceinline__ ListTop team_list(float v, bool any, ReduceLds<NT>& l) {
+  ListTop t{wave_max(v), __builtin_amdgcn_ballot_w64(any) != 0};
+  if (NT == kWave) return t;
+  if (lane_id() == 0) {
+    l.m[threadIdx.x / kWave] = t.m;
+    l.w[threadIdx.x / kWave] = t.any ? 1.0 : 0.0;
+  }
   __syncthreads();
-  v = l.w[0] != 0.0;
+  t = ListTop{l.m[0], l.w[0] != 0.0};
 #pragma unroll
-  for (int i = 1; i < NT / kWave; ++i) v |= l.w[i] != 0.0;
-  return v;
+  for (int i = 1; i < NT / kWave; ++i) {
+    t.m = fmaxf(t.m, l.m[i]);
+    t.any |= l.w[i] != 0.0;
+  }
+  return t;
 }
 template <int NT> __device__ __forceinline__ double team_sum(double v, ReduceLds<NT>& l) {
   v = wave_sum(v);
@@ -522,13 +555,10 @@ __device__ __forceinline__ RowSums part_sums(const Part<E>& part, float c, const
 // Joins sums of parts, each against the reference of its own maximum, far or
 // not, in `r`.
 template <bool W> __device__ __forceinline__ void sums_join(RowSums& r, RowSums o, float c) {
-  auto base = [&](float m) {
-    return far_row(m, c) ? (double)m * (double)c : (double)reference(m, c);
-  };
   const float m = fmaxf(r.m, o.m);
   auto to_m = [&](RowSums& a) {
     if (a.m != m && a.m != -__builtin_inff()) {   // below every entry: sums of zero, or NaN
-      const float d = (float)(base(a.m) - base(m));
+      const float d = (float)(reference64(a.m, c) - reference64(m, c));
       const double f = (double)hw_exp2(d);
       if (W) a.w = f == 0.0 ? f * a.w : f * (a.w + (double)d * a.s);
       a.s *= f;

@@ -65,3 +65,96 @@ def test_rows_without_entries(S, R, V, tail, dtype):
     for loss, grad in both_ways(S, z, ids, values, w, 1.0, tail):
         assert math.isnan(float(loss[2])) if tail else float(loss[2]) == 0.0
         assert bool(torch.isnan(grad[2]).all()) if tail else bool((grad[2] == 0).all())
+
+
+def tail_formula(z, ids, values, w):
+    """(loss, gradient, magnitude of its terms, magnitude of the loss's terms) of
+    the form with the tail at temperature 1, with log p_r as a log-sum-exp of its own
+    so that no p_r is too small for it."""
+    z, values, w = z.double(), values.double(), w.double()[:, None]
+    R, V = z.shape
+    logp = torch.log_softmax(z, -1)
+    some = ids != F.IGNORE
+    spot = torch.where(some, ids, torch.full_like(ids, V))
+    q = torch.where(some, torch.exp(values), torch.zeros_like(values))
+    qv = torch.zeros(R, V + 1, dtype=torch.float64).scatter_add_(1, spot, q)[:, :V]
+    on = torch.zeros(R, V + 1, dtype=torch.bool).scatter_(1, spot, True)[:, :V]
+    far = torch.logsumexp(logp.masked_fill(on, -math.inf), -1, keepdim=True)
+    rest = (1.0 - q.sum(-1, keepdim=True)).clamp_min(0.0)
+    at = logp.gather(1, ids.clamp_min(0))
+    loss = torch.where(some, q * (values - at), torch.zeros_like(q)).sum(-1) + (rest * (rest.log() - far))[:, 0]
+    mags = torch.where(some, q * (values.abs() + at.abs()), torch.zeros_like(q)).sum(-1) \
+        + (rest * (rest.log().abs() + far.abs()))[:, 0]
+    # (Not exp(logp - far): at 3.4e38 a difference in fp64 has no units left.)
+    share = torch.softmax(z.masked_fill(on, -math.inf), -1)
+    grad = torch.where(on, logp.exp() - qv, share * (far.exp() - rest)) * w
+    mag = torch.where(on, logp.exp() + qv, share * (far.exp() + rest)) * w.abs()
+    return loss, grad, mag, mags
+
+
+def check_tail(S, z, ids, values, w, dtype, rows):
+    ref, gref, mag, mags = tail_formula(z[rows], ids[rows], values[rows], w[rows])
+    # Each logarithm's sum is off by SUM, and the rounding of the scale
+    # log2(e) / T to fp32 moves every log p by up to 2^-24 of itself; so it
+    # does p_r in the gradient, whose ONE holds that up to 400 nats (4 ONE of
+    # a p_r below e^-400 are nothing).
+    bound = 4 * F.SUM + 2.0 ** -24 * (ref.abs() + mags)
+    for loss, grad in both_ways(S, z, ids, values, w, 1.0, True):
+        F.assert_within(loss[rows], ref, bound, "loss")
+        F.check_grad(grad[rows], gref, mag, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["160 80", "120 60", "300", "-1e4", "lowest", "far"])
+@pytest.mark.parametrize("R,V", LAYOUTS)
+def test_tail_far_below_the_list(S, R, V, kind, dtype):
+    """The probability off the list may be below fp32's range, with a listed
+    entry between the largest one and those off the list or none, finite masks
+    off the list among them: loss and gradient are finite, and depend neither on
+    the layout nor on where the listed entries stand.  Upstream gradients of a
+    scaled loss among them."""
+    g = torch.Generator().manual_seed(R + V)
+    z = torch.rand(R, V, generator=g) / 2
+    ids = torch.stack([torch.randperm(V, generator=g)[:4] for _ in range(R)])
+    ids[:, 3] = F.IGNORE
+    ids[1, 2] = F.IGNORE
+    listed = {"160 80": [160.0, 80.0, 80.5], "120 60": [120.0, 60.0, 1.0], "300": [300.0, 299.0, 298.0],
+              "-1e4": [3.0, 2.0, 1.0], "lowest": [3.0, 2.0, 1.0], "far": [3e9, 3e9, 0.0]}[kind]
+    if kind == "far" and dtype == torch.float16:
+        listed = [60000.0, 30000.0, 0.0]
+    if kind == "-1e4":
+        z -= 10000.0
+    if kind == "lowest":
+        z[:] = torch.finfo(dtype).min
+    for j, v in enumerate(listed):
+        rows = ids[:, j] != F.IGNORE
+        z[rows, ids[rows, j]] = v
+    z = z.to(dtype)
+    values = torch.log(torch.tensor([[0.5, 0.2, 0.1, 1.0]] * R))
+    w = torch.rand(R, generator=g) + 0.5
+    if dtype != torch.float16:
+        w[2], w[3] = 65536.0, -65536.0
+    check_tail(S, z, ids, values, w, dtype, list(range(6)))
+
+
+@pytest.mark.parametrize("R,V", LAYOUTS)
+@pytest.mark.parametrize("vtype", TYPES)
+def test_complete_lists_of_masked_students(S, R, V, vtype):
+    """A list of all that a student allows, the others masked by a finite
+    value: what the rounding of the list's values leaves of one does not meet
+    the masks."""
+    g = torch.Generator().manual_seed(3)
+    z = torch.full((R, V), -1e4)
+    ids = torch.stack([torch.randperm(V, generator=g)[:5] for _ in range(R)])
+    allowed = torch.randn(R, 5, generator=g)
+    z.scatter_(1, ids, allowed)
+    values = torch.log_softmax(torch.randn(R, 5, generator=g).double(), -1).to(vtype)
+    w = torch.ones(R)
+    q, logp = values.double().exp(), torch.log_softmax(allowed.double(), -1)
+    ref = (q * (values.double() - logp)).sum(-1)
+    for loss, grad in both_ways(S, z, ids, values, w, 1.0, True):
+        F.assert_within(loss, ref, 4 * F.SUM + 2.0 ** -23 * ref.abs())
+        off = torch.ones(R, V, dtype=torch.bool).scatter_(1, ids, False)
+        assert bool((grad[off] == 0).all())
+        # p - q: two exponentials of either, and the gradient's rounding
+        F.assert_within(grad.gather(1, ids), logp.exp() - q, 4 * F.ONE * (logp.exp() + q) + 2.0 ** -24)
