@@ -40,9 +40,13 @@ __device__ __forceinline__ void token_finish(const TokenArgs& a, uint32_t row, c
   const bool none = r.s == 0.0 && r.m == -__builtin_inff();
   const Exponent x = row_exponent(r.m, a.c);
   const double ln_s = none ? 0.0 : ln32(r.s);
-  // A row without any entry above -inf gives every token probability zero.
+  // A row without any entry above -inf gives every token probability zero.  An
+  // entry with all of the probability has an exponent that is what the rounding
+  // of the reference left, and an S whose exponential and logarithm are rounded:
+  // they cancel to 1e-7, on either side of zero.  (A NaN stays one.)
   auto logprob_of = [&](float z) {
-    return none ? -__builtin_inff() : (float)(kLn2 * exponent64(x, z) - ln_s);
+    const float lp = none ? -__builtin_inff() : (float)(kLn2 * exponent64(x, z) - ln_s);
+    return lp > 0.f ? 0.f : lp;
   };
   const int tid = team_tid<NT>();
   if (tid == 0) {

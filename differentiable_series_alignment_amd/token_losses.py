@@ -257,7 +257,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
     with each row's entropy and its most likely entries.
 
     ``logits`` (..., V); ``tokens`` (...) int32 or int64, or None.  Returns
-    ``TokenLogProbs``: ``logprobs`` (...) (None without tokens; 0 where the
+    ``TokenLogProbs``: ``logprobs`` (...), at most 0 (None without tokens; 0 where the
     token is ``ignore_index``, NaN where it is any other id outside the
     vocabulary), ``entropy`` (...) in nats, and with ``top_k`` (at most 128)
     ``top_logprobs`` and ``top_tokens`` (..., top_k), falling, ties to the

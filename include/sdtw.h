@@ -282,8 +282,8 @@ typedef enum {
 /* Bytes of workspace of sdtw_token_logprobs; 0 for invalid sizes. */
 size_t sdtw_token_workspace_bytes(int64_t B, int64_t N, int64_t V, int top_k);
 
-/* Log-probabilities of given tokens [B,N] (logprobs[row] = log p(token); 0
- * for an ignored one), the entropy of each row in nats, and the top_k most
+/* Log-probabilities of given tokens [B,N] (logprobs[row] = log p(token), at
+ * most 0; 0 for an ignored one), the entropy of each row in nats, and the top_k most
  * likely entries (0..128, at most V; falling, ties to the lower index; ids
  * int64): top_logprobs and top_tokens [B,N,top_k].  tokens may be NULL (then
  * logprobs is not written); stats ([B,N,4] fp32) may be NULL if no backward

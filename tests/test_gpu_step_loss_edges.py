@@ -158,3 +158,24 @@ def test_complete_lists_of_masked_students(S, R, V, vtype):
         assert bool((grad[off] == 0).all())
         # p - q: two exponentials of either, and the gradient's rounding
         F.assert_within(grad.gather(1, ids), logp.exp() - q, 4 * F.ONE * (logp.exp() + q) + 2.0 ** -24)
+
+
+@pytest.mark.parametrize("R,V", [(2000, 1), (1100, 250), (1100, 3001), (300, 3001), (9, 140001)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_log_probabilities_are_never_positive(S, R, V, dtype):
+    """One entry with all of the probability (a vocabulary of one, one allowed
+    entry, a sure row): its log-probability is at most 0, and so are the others."""
+    g = torch.Generator().manual_seed(V)
+    z = (torch.randn(R, V, generator=g) * 5).to(dtype)
+    best = torch.randint(0, V, (R, 1), generator=g)
+    top = torch.rand(R, 1, generator=g) * 40
+    z[: R // 2] = -math.inf                              # one allowed entry
+    z.scatter_(1, best, (top + 60.0).to(dtype))
+    z[-1, 0] = math.nan
+    k = min(V, 5)
+    r = S.token_logprobs(z.to(DEV), best[:, 0].to(DEV), temperature=0.7, top_k=k)
+    assert bool(torch.isnan(r.logprobs[-1])) and bool(torch.isnan(r.top_logprobs[-1]).all())
+    assert bool((r.logprobs[:-1] <= 0).all()), float(r.logprobs[:-1].max())
+    assert bool((r.top_logprobs[:-1] <= 0).all()), float(r.top_logprobs[:-1].max())
+    some = torch.arange(0, R, max(1, R // 8))
+    F.check_token_values(S.TokenLogProbs(*(x[some] for x in r)), z[some], best[some, 0], 0.7, k)
