@@ -102,6 +102,8 @@ def _walk(t: torch.Tensor, lead: int):
     """(t, stride of the outer leading dimensions as one, stride of the last
     leading dimension): t itself where two strides reach every row and the
     rest is contiguous, else a contiguous copy of it."""
+    if t.numel() == 0:
+        return t, 0, 0      # (contiguous by any strides: a copy would be the same)
     shape, stride = t.shape, t.stride()
     ok = t.dim() == lead or shape[-1] == 1 or stride[-1] == 1
     outer = 0

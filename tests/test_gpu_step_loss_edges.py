@@ -179,3 +179,18 @@ def test_log_probabilities_are_never_positive(S, R, V, dtype):
     assert bool((r.top_logprobs[:-1] <= 0).all()), float(r.top_logprobs[:-1].max())
     some = torch.arange(0, R, max(1, R // 8))
     F.check_token_values(S.TokenLogProbs(*(x[some] for x in r)), z[some], best[some, 0], 0.7, k)
+
+
+@pytest.mark.parametrize("make", [lambda: torch.empty(2, 0, 3, 8), lambda: torch.empty(0, 8, 4).transpose(1, 2),
+                                  lambda: torch.empty(3, 0, 8)])
+def test_batches_without_rows(S, make):
+    z = make().to(DEV).requires_grad_(True)
+    shape = z.shape[:-1]
+    r = S.token_logprobs(z, torch.zeros(shape, dtype=torch.int64, device=DEV), top_k=2)
+    assert r.logprobs.shape == shape and r.top_tokens.shape == (*shape, 2)
+    ids = torch.zeros(*shape, 3, dtype=torch.int32, device=DEV)
+    loss = S.distillation_loss(z, ids, torch.zeros(*shape, 3, device=DEV), tail=True)
+    (r.logprobs.sum() + r.entropy.sum() + r.top_logprobs.sum() + loss.sum()).backward()
+    assert loss.shape == shape and z.grad.shape == z.shape
+    loss, grad = S.distillation_value_and_grad(z, ids, torch.zeros(*shape, 3, device=DEV))
+    assert loss.shape == shape and grad.shape == z.shape
