@@ -73,6 +73,7 @@ template <int NT> struct alignas(16) DistillLds {
   static constexpr int kList = NT < 256 ? kListWave : kListMax;
   int ids[kList];
   float q[kList];
+  int twice;       // whether an id stands twice (TAIL)
 };
 
 // The calling thread's entry of the list, loaded early.
@@ -253,11 +254,11 @@ template <typename E, bool TAIL, bool GRAD, int HG, bool ALL, int NT, bool ONCE>
 __global__ __launch_bounds__(kTeamBlock<NT>) void
 k_distill_rows(DistillArgs a) {
   __shared__ ReduceLds<NT> red;          // (a wave reduces in registers)
-  __shared__ DistillLds<NT> lists[GRAD ? kTeams<NT> : 1];
+  __shared__ DistillLds<NT> lists[GRAD || TAIL ? kTeams<NT> : 1];
   extern __shared__ uint32_t bits[];     // TAIL: a bit for each entry of the part
   const uint32_t words = bitmap_words<E>(a.split.len);
   uint32_t* listed = bits + team_id<NT>() * words;
-  DistillLds<NT>& l = lists[GRAD ? team_id<NT>() : 0];
+  DistillLds<NT>& l = lists[GRAD || TAIL ? team_id<NT>() : 0];
   const uint32_t tid = team_tid<NT>();
   const uint64_t items = (uint64_t)a.in.rows * a.split.parts;
   const uint64_t item = a.first + (uint64_t)blockIdx.x * kTeams<NT> + team_id<NT>();
@@ -276,12 +277,19 @@ k_distill_rows(DistillArgs a) {
   bool first = true;
   if (TAIL) {
     for (uint32_t i = tid; i < words; i += NT) listed[i] = 0;
+    if (tid < DistillLds<NT>::kList) l.ids[tid] = id;
+    if (tid == 0) l.twice = 0;
     team_sync<NT>();
+    stress_delay(64);
     if (id >= (int)lo && id < (int)hi) {
       const uint32_t at = p.bit(id - lo), bit = 1u << (at & 31);
-      first = !(atomicOr(&listed[at >> 5], bit) & bit);
+      if (atomicOr(&listed[at >> 5], bit) & bit) l.twice = 1;
     }
     team_sync<NT>();
+    // Of equal ids the first one counts, not the one whose wave came first: the
+    // order of the list's sum goes by the list alone.
+    if (l.twice && id >= 0)
+      for (int j = 0; j < (int)tid; ++j) first &= l.ids[j] != id;
   }
   const ListEntry e = list_entry<E>(a, row, tid, id);
   float mine;

@@ -137,34 +137,6 @@ __device__ __forceinline__ bool release_ctrl(unsigned* ctrl, int64_t nprog, bool
   return s_last;
 }
 
-// Hand-off stress (debug builds only: SDTW_STRESS=1, built as
-// libsdtw_stress.so).  Every producer's publish, every consumer's wait and
-// every pass of a hand-off wave first sleeps a pseudo-random time: mostly
-// 0-3 sleeps of 8 x 64 clocks, one time in eight up to 63 of them (about
-// 13 us).  The hash mixes the clock with the site, workgroup and wave, so
-// producers and consumers drift against each other differently on every
-// run; results must not change, only timings.  In normal builds it is empty.
-#ifndef SDTW_STRESS
-#define SDTW_STRESS 0
-#endif
-__device__ __forceinline__ void stress_delay(unsigned site) {
-#if SDTW_STRESS
-  const uint64_t t = __builtin_readcyclecounter();
-  uint32_t h = (uint32_t)t ^ (uint32_t)(t >> 32) ^ (site * 0x9E3779B9u) ^
-               (blockIdx.x * 0x85EBCA6Bu) ^ ((threadIdx.x >> 6) * 0xC2B2AE35u);
-  h ^= h >> 15;
-  h *= 0x2C1B3C6Du;
-  h ^= h >> 12;
-  h *= 0x297A2D39u;
-  h ^= h >> 15;
-  h = __builtin_amdgcn_readfirstlane(h);
-  const uint32_t n = (h & 7u) == 0u ? (h >> 3) & 63u : (h >> 3) & 3u;
-  for (uint32_t i = 0; i < n; ++i) __builtin_amdgcn_s_sleep(8);
-#else
-  (void)site;
-#endif
-}
-
 // ---------------------------------------------------------------------------
 // Decoupled bands.  Inside a workgroup every band wave runs at its own pace;
 // the row a band hands to the band below travels through an LDS ring of

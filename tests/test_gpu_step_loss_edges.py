@@ -194,3 +194,31 @@ def test_batches_without_rows(S, make):
     assert loss.shape == shape and z.grad.shape == z.shape
     loss, grad = S.distillation_value_and_grad(z, ids, torch.zeros(*shape, 3, device=DEV))
     assert loss.shape == shape and grad.shape == z.shape
+
+
+@pytest.mark.parametrize("R,V,K", [(2000, 4000, 256), (300, 20011, 250), (1100, 500, 64)])
+def test_repeated_ids_give_the_same_bits(S, monkeypatch, R, V, K):
+    """A list whose ids stand several times, their copies in different waves:
+    which of them counts in p does not go by the order in which waves get there
+    (the build with pseudo-random delays mixes it).  The student is near the
+    teacher, so that the loss is as small as its sums' last bits."""
+    from differentiable_series_alignment_amd import _lib
+    g = torch.Generator().manual_seed(K)
+    z = torch.randn(R, V, generator=g) * 8     # (a narrow range of exponentials sums exactly)
+    ids = torch.stack([torch.randperm(V, generator=g)[:K // 2].repeat(2)[torch.randperm(K, generator=g)]
+                       for _ in range(R)])
+    values = (torch.log_softmax(z.double(), -1).gather(1, ids) - math.log(2.0)).float()
+    w = torch.rand(R, generator=g) + 0.5
+    args = [x.to(DEV) for x in (z, ids, values, w)]
+    loss, grad = S.distillation_value_and_grad(*args, tail=True)
+    some = list(range(0, R, R // 6))
+    ref, gref, mag, mags = F.distill(z[some], ids[some], values[some], 1.0, True, w[some])
+    F.assert_within(loss[some], ref, 4 * F.SUM + 2.0 ** -24 * ref.abs() + 1e-12 * mags)
+    F.check_grad(grad[some].cpu(), gref, mag, torch.float32)
+    plain = S.distillation_loss(*args[:3], tail=True)
+    monkeypatch.setattr(_lib, "_lib", _lib.load(_lib.STRESS_LIB_PATH))
+    for _ in range(8):
+        loss1, grad1 = S.distillation_value_and_grad(*args, tail=True)
+        assert torch.equal(loss, loss1), int((loss != loss1).sum())
+        assert torch.equal(grad, grad1)
+        assert torch.equal(plain, S.distillation_loss(*args[:3], tail=True))
