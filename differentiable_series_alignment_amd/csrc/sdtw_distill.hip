@@ -138,7 +138,8 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   const bool none = sum == 0.0 && m == -__builtin_inff();
   double rest = TAIL && teacher ? 1.0 - qsum : 0.0;
   if (rest < 0.0) rest = 0.0;
-  const double left = TAIL && !none ? share / sum : 0.0;
+  const double inv = none ? 0.0 : 1.0 / sum;
+  const double left = TAIL ? share * inv : 0.0;
   // One evaluation of the logarithm, on four lanes.
   const int lane = lane_id();
   const double lns = log(lane == 0 ? sum : lane == 1 ? qsum : lane == 2 ? rest : r.s);
@@ -155,7 +156,7 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   if (e.id == -2) part = __builtin_nan("");
   team_sync<NT>();
   double loss = team_sum<NT>(part, l);
-  double off = none || !teacher ? 0.0 : 1.0 / sum;
+  double off = teacher ? inv : 0.0;
   if (TAIL && teacher) {
     if (left < 0x1p-126 && !none) {
       // Next to nothing off the list for the rest to fall on: what the rounding
@@ -173,8 +174,7 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   }
   if (__builtin_isnan(loss)) off = __builtin_nan("");
   if (none) qscale = 0.0;
-  const float inv_s = none ? 0.f : (float)(1.0 / sum);
-  const DistillStats st{x.ref, inv_s, none ? 0.f : (float)off, tmax, (float)tscale,
+  const DistillStats st{x.ref, (float)inv, none ? 0.f : (float)off, tmax, (float)tscale,
                         (float)qscale, (x.far ? 1.f : 0.f) + (y.far ? 2.f : 0.f), y.ref};
   if (tid == 0) {
     a.loss[row] = (float)loss;
