@@ -159,13 +159,16 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
   double off = teacher ? inv : 0.0;
   if (TAIL && teacher) {
     if (left < 0x1p-126 && !none) {
-      // Next to nothing off the list for the rest to fall on: what the rounding
-      // of the list's values (half a step of their type each) can make of a
-      // list that is complete is no rest.
+      // Next to nothing off the list for the rest to fall on: what roundings can
+      // make of a list that is complete is no rest.  Its values are off by half
+      // a step of their type each, and all of them together by what fp32 leaves
+      // of the log-sum-exp that was taken from them: half a step of it, up to
+      // 2^-19 for logits up to 64, and as much again for its sum.
       const double half = a.list.bytes == SDTW_DTYPE_F32    ? 0x1p-24
                           : a.list.bytes == SDTW_DTYPE_BF16 ? 0x1p-8 : 0x1p-11;
       team_sync<NT>();
-      if (rest <= half * (1.0 + team_sum<NT>(q == 0.0 ? 0.0 : q * fabs(logq), l))) rest = 0.0;
+      if (rest <= 0x1p-18 + half * (1.0 + team_sum<NT>(q == 0.0 ? 0.0 : q * fabs(logq), l)))
+        rest = 0.0;
     }
     if (rest != 0.0)
       loss += rest * (lane_value(lns, 2) - (lane_value(lns, 3) + kLn2 * down - ln_s));

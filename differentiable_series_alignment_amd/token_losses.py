@@ -360,7 +360,10 @@ def distillation_loss(logits: torch.Tensor, teacher_tokens: torch.Tensor,
     teacher's log-probabilities at this temperature over its whole vocabulary,
     and what they leave is one more class: the loss adds q_r (log q_r -
     log p_r) with q_r = 1 - sum q and p_r the student's probability off the
-    list.  The factor temperature^2 that some recipes apply is the caller's.
+    list.  Where that is nothing (below 2^-126: a list of every entry, or the
+    others masked), a q_r no larger than the roundings behind the values counts
+    as zero; a larger one is a loss of +inf if there is no other entry at all.
+    The factor temperature^2 that some recipes apply is the caller's.
 
     Differentiable in the logits; the teacher is constant.  An id listed twice
     adds in q and counts once in p; an id outside the vocabulary makes its row

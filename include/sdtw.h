@@ -325,7 +325,8 @@ size_t sdtw_distill_workspace_bytes(int64_t B, int64_t N, int64_t V, int K);
  *     is one more class for both sides: loss += q_r (log q_r - log p_r) with
  *     p_r the probability off the list, however small (zero if nothing there is
  *     above -inf; where it is below 2^-126, a q_r that the rounding of the
- *     values explains counts as zero).
+ *     values explains, or one up to 2^-18, which that of an fp32 log-sum-exp
+ *     behind them does, counts as zero: a list of all entries is complete).
  * An id listed twice adds in q and counts once in p.  A row without entries
  * (nothing but padding; with tail = 0 also values of -inf alone) has loss 0
  * and gradient 0 whatever its logits, -inf, +inf and NaN among them, and

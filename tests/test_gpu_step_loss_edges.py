@@ -222,3 +222,26 @@ def test_repeated_ids_give_the_same_bits(S, monkeypatch, R, V, K):
         assert torch.equal(loss, loss1), int((loss != loss1).sum())
         assert torch.equal(grad, grad1)
         assert torch.equal(plain, S.distillation_loss(*args[:3], tail=True))
+
+
+@pytest.mark.parametrize("vtype", TYPES)
+@pytest.mark.parametrize("R,V", [(2000, 100), (9, 100)])
+def test_complete_lists_of_computed_log_probabilities(S, R, V, vtype):
+    """A teacher's log-probabilities over the whole vocabulary, computed in
+    fp32: their log-sum-exp near 30 is off by up to half a step there, 2^-20,
+    and so is the list's sum.  That is no class of its own, also where the
+    teacher is sure."""
+    g = torch.Generator().manual_seed(R)
+    t = torch.randn(R, V, generator=g) * 2 + 15
+    t[:, 3] = 30.0 + torch.rand(R, generator=g)
+    z = torch.randn(R, V, generator=g)
+    ids = torch.arange(V).repeat(R, 1)
+    own = S.token_logprobs(t.to(DEV), top_k=V)
+    plain = t - torch.logsumexp(t, -1, keepdim=True)
+    for i, v in ((own.top_tokens.cpu(), own.top_logprobs.cpu()), (ids, plain)):
+        v = v.to(vtype)
+        q = torch.exp(v.double())
+        ref = (q * (v.double() - torch.log_softmax(z.double(), -1).gather(1, i))).sum(-1)
+        for loss, grad in both_ways(S, z, i, v, torch.ones(R), 1.0, True):
+            F.assert_within(loss, ref, 4 * F.SUM + 2.0 ** -23 * ref.abs())
+            assert bool(torch.isfinite(grad).all())
