@@ -27,3 +27,39 @@ def test_walks():
         flat = w.as_strided((w.untyped_storage().nbytes() // 4 - w.storage_offset(),), (1,))
         rows = [flat[(r // n) * outer + (r % n) * inner:][:t.shape[-1]] for r in range(t[..., 0].numel())]
         assert torch.equal(torch.stack(rows), t.reshape(-1, t.shape[-1]))
+
+
+CALLS = [lambda z, i, v: S.token_logprobs(z, i[:, 0]), lambda z, i, v: S.token_logprobs(z, top_k=2),
+         S.distillation_loss, S.distillation_value_and_grad, S.DistillationLoss()]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_forward_mode_is_refused(call):
+    """A tangent would be lost without a word."""
+    import torch.autograd.forward_ad as fw
+    z, i, v = torch.randn(2, 10), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    with fw.dual_level():
+        dual = fw.make_dual(z, torch.ones_like(z))
+        with pytest.raises(ValueError, match="forward-mode"):
+            call(dual, i, v)
+        with pytest.raises(ValueError, match="forward-mode"):
+            call(dual.clone().requires_grad_(True), i, v)
+        with pytest.raises(ValueError, match="GPU"):       # no tangent, no refusal of that kind
+            call(z, i, v)
+        with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+            call(dual, i, v)
+    with pytest.raises(ValueError, match="forward-mode"):
+        torch.func.jvp(lambda x: call(x, i, v), (z,), (torch.ones_like(z),))
+
+
+def test_forward_mode_of_what_goes_beside_is_refused():
+    import torch.autograd.forward_ad as fw
+    z, i, v = torch.randn(2, 10), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    with fw.dual_level():
+        dual = fw.make_dual(v, torch.ones_like(v))
+        for call in CALLS[2:]:
+            with pytest.raises(ValueError, match="forward-mode"):
+                call(z, i, dual)
+        w = fw.make_dual(torch.ones(2), torch.ones(2))
+        with pytest.raises(ValueError, match="forward-mode"):
+            S.distillation_value_and_grad(z, i, v, w)
