@@ -89,6 +89,17 @@ def _check_logits(logits, temperature) -> float:
     return t
 
 
+def _check_ignore(ignore_index) -> int:
+    try:
+        i = int(ignore_index)
+        ok = i == ignore_index and -(1 << 63) <= i < 1 << 63
+    except (TypeError, ValueError, OverflowError):
+        ok = False
+    if not ok:
+        raise ValueError(f"ignore_index must be an integer of 64 bits, got {ignore_index}")
+    return i
+
+
 def _check_device(logits):
     # Last of the checks, so that the others can be met without a GPU.
     if logits.device.type != "cuda":
@@ -284,17 +295,19 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
     V = logits.shape[-1]
     if k != top_k or not 0 <= k <= min(TOP_K_MAX, V):
         raise ValueError(f"top_k must be an integer from 0 to min({TOP_K_MAX}, V = {V}), got {top_k}")
+    ignore = _check_ignore(ignore_index)
     if tokens is not None:
         _check_beside("tokens", tokens, logits, logits.shape[:-1], _ID_BYTES)
     _check_device(logits)
     if torch.is_grad_enabled() and logits.requires_grad:
-        out = _TokenLogProbsFunction.apply(logits, tokens, t, k, int(ignore_index))
+        out = _TokenLogProbsFunction.apply(logits, tokens, t, k, ignore)
         return TokenLogProbs(*out)
-    return TokenLogProbs(*_token_forward(logits, tokens, t, k, int(ignore_index), False)[:4])
+    return TokenLogProbs(*_token_forward(logits, tokens, t, k, ignore, False)[:4])
 
 
-def _check_distill(logits, ids, values, temperature, weights=None):
+def _check_distill(logits, ids, values, temperature, ignore_index, weights=None):
     t = _check_logits(logits, temperature)
+    ignore = _check_ignore(ignore_index)
     if not isinstance(ids, torch.Tensor) or ids.dim() < 1:
         raise ValueError("teacher_tokens must be a tensor (..., K)")
     K = ids.shape[-1]
@@ -310,7 +323,7 @@ def _check_distill(logits, ids, values, temperature, weights=None):
         _check_beside("weights", weights, logits, logits.shape[:-1], (torch.float32,))
         _check_tangent("weights", weights)
     _check_device(logits)
-    return t
+    return t, ignore
 
 
 def _distill(r, t, tail, ignore_index, loss, stats, gl, grad):
@@ -383,14 +396,14 @@ def distillation_loss(logits: torch.Tensor, teacher_tokens: torch.Tensor,
     adds in q and counts once in p; an id outside the vocabulary makes its row
     NaN.  A row without entries has loss 0 and gradient 0, whatever its logits
     hold."""
-    t = _check_distill(logits, teacher_tokens, teacher_logits, temperature)
+    t, ignore = _check_distill(logits, teacher_tokens, teacher_logits, temperature, ignore_index)
     if torch.is_grad_enabled() and logits.requires_grad:
         return _DistillationFunction.apply(logits, teacher_tokens, teacher_logits, t,
-                                           int(bool(tail)), int(ignore_index))
+                                           int(bool(tail)), ignore)
     with _on(logits.device):
         loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-        _distill(_rows(logits, teacher_tokens, teacher_logits), t, int(bool(tail)),
-                 int(ignore_index), loss, None, None, None)
+        _distill(_rows(logits, teacher_tokens, teacher_logits), t, int(bool(tail)), ignore,
+                 loss, None, None, None)
     return loss
 
 
@@ -405,7 +418,8 @@ def distillation_value_and_grad(logits: torch.Tensor, teacher_tokens: torch.Tens
     fill the GPU.  For training steps that know each row's weight beforehand
     (1 / rows for a mean); ``logits.backward(grad)`` then continues below the
     head.  ``weights`` (...) float32, or None for ones; no graph is recorded."""
-    t = _check_distill(logits, teacher_tokens, teacher_logits, temperature, weights)
+    t, ignore = _check_distill(logits, teacher_tokens, teacher_logits, temperature, ignore_index,
+                               weights)
     dev = logits.device
     with _on(dev), torch.no_grad():
         r = _rows(logits, teacher_tokens, teacher_logits)
@@ -414,7 +428,7 @@ def distillation_value_and_grad(logits: torch.Tensor, teacher_tokens: torch.Tens
         stats = None
         if r.V > L.SDTW_ROWS_WHOLE:       # split rows pass their statistics on
             stats = torch.empty((r.B * r.N, 8), dtype=torch.float32, device=dev)
-        _distill(r, t, int(bool(tail)), int(ignore_index), loss, stats, weights, grad)
+        _distill(r, t, int(bool(tail)), ignore, loss, stats, weights, grad)
     return loss, grad
 
 
@@ -430,7 +444,7 @@ class DistillationLoss(torch.nn.Module):
             raise ValueError(f"temperature must be within [1e-6, 1e6], got {temperature}")
         self.temperature = t
         self.tail = bool(tail)
-        self.ignore_index = int(ignore_index)
+        self.ignore_index = _check_ignore(ignore_index)
 
     def forward(self, logits, teacher_tokens, teacher_logits):
         return distillation_loss(logits, teacher_tokens, teacher_logits, self.temperature,

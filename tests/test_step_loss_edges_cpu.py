@@ -63,3 +63,25 @@ def test_forward_mode_of_what_goes_beside_is_refused():
         w = fw.make_dual(torch.ones(2), torch.ones(2))
         with pytest.raises(ValueError, match="forward-mode"):
             S.distillation_value_and_grad(z, i, v, w)
+
+
+@pytest.mark.parametrize("bad", [1 << 63, -(1 << 63) - 1, (1 << 64) - 100, -100.5, float("nan"), float("inf"), None, "x"])
+def test_ignore_index_is_an_int64(bad):
+    """One that wraps to another id, or is rounded to one, would drop that id."""
+    z, i, v = torch.randn(2, 10), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    for call in (lambda: S.token_logprobs(z, i[:, 0], ignore_index=bad),
+                 lambda: S.distillation_loss(z, i, v, ignore_index=bad),
+                 lambda: S.distillation_value_and_grad(z, i, v, ignore_index=bad),
+                 lambda: S.DistillationLoss(ignore_index=bad)):
+        with pytest.raises(ValueError, match="ignore_index"):
+            call()
+
+
+@pytest.mark.parametrize("good", [0, -100, -100.0, (1 << 63) - 1, -(1 << 63), True])
+def test_ignore_index_of_other_kinds(good):
+    z, i, v = torch.randn(2, 10), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    assert S.DistillationLoss(ignore_index=good).ignore_index == int(good)
+    with pytest.raises(ValueError, match="GPU"):
+        S.token_logprobs(z, i[:, 0], ignore_index=good)
+    with pytest.raises(ValueError, match="GPU"):
+        S.distillation_value_and_grad(z, i, v, ignore_index=good)
