@@ -249,7 +249,7 @@ __device__ __forceinline__ void distill_grad(const DistillArgs& a, uint32_t row,
 // Values: bound by memory, and by the row's own chain (list, sums, logarithms)
 // where rows are short.  4096 rows of 131072 (bf16), K = 64: 163 us, 6.6 TB/s;
 // with the tail 183, since its list has to be in the bitmap before the first
-// sum.  2048 rows of 50016: 40 us, with the tail 44.  With the gradient: 455 us
+// sum.  2048 rows of 50016: 41 us, with the tail 46.  With the gradient: 455 us
 // for the 4096, against 163 + 350 in two launches; 1.8 GiB read and 1 written,
 // bound by the last-level cache and memory together.  513 rows of 65537
 // (fp16), K = 128: 40 us.
@@ -361,6 +361,9 @@ k_distill_grad(DistillArgs a) {
     const int64_t i = id_load(a.ids, a.in.rows, a.in.n, row, tid);
     if (i != a.ignore && i >= 0 && i < (int64_t)a.in.V) {
       id = (int)i;
+      // (fp32, where the one call's q is fp64: four roundings leave the exponent
+      // u <= 0 off by up to 2^-22 of itself, which moves q by at most
+      // |u| e^u 2^-22 < 2^-23; an fp64 exponential would be each team's of a row.)
       q = __expf((list_load(a, row, tid) - st.tmax) * st.tscale) * st.qscale;
     }
   }

@@ -893,13 +893,15 @@ inline float make_scale(double temperature) { return (float)(kLog2e / temperatur
 // maxima, for the top entries, are 16 KiB of 16-bit logits and 32 of fp32),
 // `parts` blocks with `len` entries each, joined by a second kernel.
 // `wave`: longest row that a wave takes by itself (4096 rows of 4096: 10 us by
-// waves, 17 by blocks of 256).  Blocks of 512 where a CU (of 256) has one row
-// at most: loss and gradient of 200 rows of 65537 take 19.4 us by 512 and 22.0
+// waves, 17 by blocks of 256).  Blocks of 512 where a CU (of an MI355X's 256)
+// has one row at most: loss and gradient of 200 rows of 65537 take 19.4 us by 512 and 22.0
 // by 256, their values 10 by both; 256 rows of 131072 38.1 and 39.9, values
 // 16.4 and 14.9.  With more rows, blocks of 256: 300 rows of 65537 take 29.6 us
 // against 32.2, 511 rows of 131072 60 against 68, values 25 against 29, 700 of
-// 65537 41 against 53.  One row of 131072 is one block's work too: 13 us, and
-// 13.6 in parts with their join.
+// 65537 41 against 53.  (At 65537 entries blocks of either size read a part of a
+// row twice; whether 512 threads that hold all of it would win is not measured.)
+// One row of 131072 is one block's work too: 13 us, and 13.6 in parts with their
+// join; a few rows of that length were not compared.
 constexpr uint32_t kPartMax = SDTW_ROWS_WHOLE;
 struct Split {
   uint32_t parts, len;

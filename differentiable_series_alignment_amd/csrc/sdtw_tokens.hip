@@ -77,7 +77,7 @@ __device__ __forceinline__ void token_finish(const TokenArgs& a, uint32_t row, c
 // Each entry takes a conversion, a maximum, an fma, an exponential (two issue
 // slots), a sum and an fma for W: bound by memory where 16-bit rows come from
 // HBM, and within a tenth by issue.  4096 rows of 131072 (bf16): 165 us, 6.5
-// TB/s of the 7.0 that a kernel reaches which only reads; with the top 64 of
+// TB/s (157 us, 6.8, at its best); with the top 64 of
 // each 2048: 112 us, 4.8 TB/s; 1024 rows of 65537 (fp16, in the last-level
 // cache) with the top 5: 34 us.  One row of 32768 with the top 20: 11 us, of
 // which 6 are the launch as events see it: the chain of one row's read, its

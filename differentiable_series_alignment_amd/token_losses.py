@@ -413,9 +413,12 @@ def distillation_value_and_grad(logits: torch.Tensor, teacher_tokens: torch.Tens
                                 temperature: float = 1.0, tail: bool = False,
                                 ignore_index: int = -100):
     """(loss, grad): ``distillation_loss`` per row (unweighted) and the
-    gradient of sum(weights * loss) with respect to the logits, in one call
-    that reads the logits from memory once where there are rows enough to
-    fill the GPU.  For training steps that know each row's weight beforehand
+    gradient of sum(weights * loss) with respect to the logits, in one call.
+    Up to 131072 entries a row that is one launch: what a block holds of its row
+    in registers (32768 entries of 16 bits, 16384 of 32, with 256 threads) is read
+    once, the rest twice, the second time from the last-level cache where it
+    still is there.  Longer rows take three launches and are read twice.  For
+    training steps that know each row's weight beforehand
     (1 / rows for a mean); ``logits.backward(grad)`` then continues below the
     head.  ``weights`` (...) float32, or None for ones; no graph is recorded."""
     t, ignore = _check_distill(logits, teacher_tokens, teacher_logits, temperature, ignore_index,
