@@ -188,7 +188,8 @@ __device__ __forceinline__ DistillStats distill_finish(const DistillArgs& a, uin
 
 // Writes the gradient of a part of a row, first as of entries off the list
 // (whose reference a listed entry may exceed by any amount: what is written for
-// it is whatever comes of that), then the list's own.  `id` is the calling thread's entry of the
+// it is whatever comes of that), then the list's own.  `id` is the calling
+// thread's entry of the
 // list (-1: none), whose ids and probabilities are in l behind a team_sync.
 // The first HG groups (ALL: there are no more) are in `held` already.
 template <typename E, int NT, bool ONCE, int HG, bool ALL>
